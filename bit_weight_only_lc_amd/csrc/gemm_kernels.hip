@@ -100,7 +100,7 @@ struct GemmArgs {
   // partial tiles are indexed x * hyb_L + (i - hyb_F).
   int hyb_per, hyb_F, hyb_L;
   int bpt;                     // forward: tile rows along P, 256 or 128 (host side)
-  int fine;                    // dW: three-part epilogue (host side)
+  int fine;                    // dW, dX: three-part epilogue (host side)
 };
 
 __device__ __forceinline__ int swz(int row) { return (row ^ (row >> 3)) & 7; }
@@ -410,9 +410,14 @@ __device__ __forceinline__ void store_block_rows64(const float* S, void* out, in
 // of C kept); the results go through the wave's LDS area only for the transposed store.
 // Blocks are taken in pairs along k, so that each output row receives 128 contiguous
 // bytes (bf16) per store instruction.
+// FINE: three bf16 parts each (24 bits) of C and of the mix, and the products kept that
+// epilogue_dw's FINE keeps, so that the mix is as exact as the float32 sums before it
+// (lcvq_linear_bwd_ckpt8, whose layers of few tiles mix in float32). Against a float32
+// product bf16 dX moves by 7e-5 of its norm, with two parts by 1.9e-4; the backward of 4096
+// tokens, 4096 x 4096, takes 1 to 2 us more of 250.
 constexpr int DX_WAVE_LDS = 64 * SROW * 4;   // per-wave staging area: 64 x 33 floats
 
-template <int D, int WI, int WJ>
+template <int D, int WI, int WJ, bool FINE>
 __device__ __forceinline__ void epilogue_dx(const GemmArgs& a, f32x16 acc[WI][WJ], int p0, int q0, int wp, int wq,
                             int lane, float* S, const float* Alds) {
   static_assert(WI % 2 == 0, "k blocks are staged in pairs");
@@ -421,7 +426,7 @@ __device__ __forceinline__ void epilogue_dx(const GemmArgs& a, f32x16 acc[WI][WJ
   // 8t .. 8t+7 (slot e: row k = 16t + 8(e/4) + 4h + e%4 of C), the entry 2 A[q % d][k % d]
   // of 2 (I kron A) inside q's d-vector, else 0, as bf16 hi + lo halves. (d = 16: A from its
   // LDS copy.)
-  bf16x8 AMh[2], AMl[2];
+  bf16x8 AMh[2], AMl[2], AMr[2];
 #pragma unroll
   for (int t = 0; t < 2; ++t)
 #pragma unroll
@@ -432,7 +437,9 @@ __device__ __forceinline__ void epilogue_dx(const GemmArgs& a, f32x16 acc[WI][WJ
       const float m = k / D == q / D ? 2.f * av : 0.f;
       const __bf16 mh = (__bf16)m;
       AMh[t][e] = mh;
-      AMl[t][e] = (__bf16)(m - (float)mh);
+      const __bf16 ml = (__bf16)(m - (float)mh);
+      AMl[t][e] = ml;
+      if constexpr (FINE) AMr[t][e] = (__bf16)(m - (float)mh - (float)ml);
     }
   // Row terms B[i] - 4 sum_j A[i][j] of this lane's output rows: register r holds row
   // 8(r/4) + 4h + r%4, i.e. i = that row mod d, slot rslot(r).
@@ -490,6 +497,21 @@ __device__ __forceinline__ void epilogue_dx(const GemmArgs& a, f32x16 acc[WI][WJ
         o = __builtin_amdgcn_mfma_f32_32x32x16_bf16(AMl[1], Ch1, o, 0, 0, 0);
         o = __builtin_amdgcn_mfma_f32_32x32x16_bf16(AMh[0], Cl0, o, 0, 0, 0);
         o = __builtin_amdgcn_mfma_f32_32x32x16_bf16(AMh[1], Cl1, o, 0, 0, 0);
+        if constexpr (FINE) {
+          uint32_t cr[8];
+#pragma unroll
+          for (int p = 0; p < 8; ++p)
+            cr[p] = pack_bf16x2(c[2 * p] - bf16lo_to_f32(ch[p]) - bf16lo_to_f32(cl[p]),
+                                c[2 * p + 1] - bf16hi_to_f32(ch[p]) - bf16hi_to_f32(cl[p]));
+          const bf16x8 Cr0 = __builtin_bit_cast(bf16x8, u32x4{cr[0], cr[1], cr[2], cr[3]});
+          const bf16x8 Cr1 = __builtin_bit_cast(bf16x8, u32x4{cr[4], cr[5], cr[6], cr[7]});
+          o = __builtin_amdgcn_mfma_f32_32x32x16_bf16(AMl[0], Cl0, o, 0, 0, 0);
+          o = __builtin_amdgcn_mfma_f32_32x32x16_bf16(AMl[1], Cl1, o, 0, 0, 0);
+          o = __builtin_amdgcn_mfma_f32_32x32x16_bf16(AMr[0], Ch0, o, 0, 0, 0);
+          o = __builtin_amdgcn_mfma_f32_32x32x16_bf16(AMr[1], Ch1, o, 0, 0, 0);
+          o = __builtin_amdgcn_mfma_f32_32x32x16_bf16(AMh[0], Cr0, o, 0, 0, 0);
+          o = __builtin_amdgcn_mfma_f32_32x32x16_bf16(AMh[1], Cr1, o, 0, 0, 0);
+        }
         float* Sh = S + half * 32 * SROW;
 #pragma unroll
         for (int r = 0; r < 16; ++r)
@@ -677,7 +699,8 @@ __device__ __forceinline__ void wait_vm_stages(int stages_after) {
 // FWD and dX: NW waves (4 or 8), 4-slot ring of direct global->LDS loads.
 // SPL: 0 one workgroup per tile; 1 phase 1 of a split launch (forward only; phase 2 is
 // k_gemm_fwd_epi). BPT: tile rows along P (128 only for the forward without a split).
-template <int OP, int D, int NW, int SPL = 0, int BPT = 256>
+// FINE: dX with the three-part mix.
+template <int OP, int D, int NW, int SPL = 0, int BPT = 256, bool FINE = false>
 __global__ __launch_bounds__(NW * 64, 1) __attribute__((amdgpu_waves_per_eu(NW / 4, NW / 4)))
 void k_gemm_ring(GemmArgs a) {
   static_assert(SPL == 0 || (SPL == 1 && OP == OP_FWD), "phase 2 of a split forward is k_gemm_fwd_epi");
@@ -799,8 +822,8 @@ void k_gemm_ring(GemmArgs a) {
                                   (tile < NOUT ? tile : 0)
                             : a.A;
     const float fv = *fsrc;
-    epilogue_dx<D, WI, WJ>(a, acc, p0, q0, wp, wq, lane,
-                           reinterpret_cast<float*>(smem + wave * DX_WAVE_LDS), Alds);
+    epilogue_dx<D, WI, WJ, FINE>(a, acc, p0, q0, wp, wq, lane,
+                                 reinterpret_cast<float*>(smem + wave * DX_WAVE_LDS), Alds);
     // wave sums at 128 KiB: above the staging areas and the copy of A
     if (a.red_partials)
       reduce_dw_partials<D, NW * 64>(a, tile, a.ntiles, tid,
@@ -1738,6 +1761,16 @@ static hipError_t launch_op(GemmArgs& a, int d, hipStream_t s) {
     }
   }
   if constexpr (OP == OP_DX) {
+    if (a.fine) {
+      constexpr int NW = LCVQ_DX_WAVES;
+      const dim3 g(((a.ntiles + 7) / 8) * 8), b(NW * 64);
+      switch (d) {
+        case 4: LCVQ_LAUNCH(PROF_DX, (k_gemm_ring<OP_DX, 4, NW, 0, 256, true>), g, b, 0, s, a); break;
+        case 8: LCVQ_LAUNCH(PROF_DX, (k_gemm_ring<OP_DX, 8, NW, 0, 256, true>), g, b, 0, s, a); break;
+        default: LCVQ_LAUNCH(PROF_DX, (k_gemm_ring<OP_DX, 16, NW, 0, 256, true>), g, b, 0, s, a); break;
+      }
+      return hipGetLastError();
+    }
     return launch_op1<OP, 0>(a, d, ((a.ntiles + 7) / 8) * 8, s);
   } else {
     if (a.hyb_L) {
@@ -1914,8 +1947,9 @@ hipError_t launch_gemm_fwd(const uint16_t* xs, const uint16_t* xs_lo, const uint
 hipError_t launch_gemm_dx(const uint32_t* r16t, const uint16_t* dy, const uint16_t* dy_lo,
                           const float* r, const float* A, const float* B, int M, int N, int K,
                           int d, void* dX, bool f32, const float* dw_partials, float* dA,
-                          float* dB, hipStream_t s) {
+                          float* dB, hipStream_t s, bool fine) {
   GemmArgs a = {};
+  a.fine = fine;
   if (dw_partials) {                         // the dW product's tiles: ceil(K/BT) x ceil(N/BT)
     a.red_partials = dw_partials;
     a.red_tiles = dw_partial_rows(M, N, K);

@@ -358,7 +358,7 @@ lcvq_status_t linear_bwd_impl(const void* dY, const void* X, const int8_t* Xc, c
   if (e != hipSuccess) return LCVQ_ERR_HIP;
   if (dX) {
     e = launch_gemm_dx(r16t, dyb, dy_lo, r, A, B, (int)M, (int)N, (int)K, d, dX, f32, partials,
-                       dA, dB, s);
+                       dA, dB, s, ckpt);
     if (e != hipSuccess) return LCVQ_ERR_HIP;
   }
   return LCVQ_OK;

@@ -89,9 +89,9 @@ hipError_t launch_gemm_fwd(const uint16_t* xs, const uint16_t* xs_lo, const uint
 hipError_t launch_gemm_dx(const uint32_t* r16t, const uint16_t* dy, const uint16_t* dy_lo,
                           const float* r, const float* A, const float* B, int M, int N, int K,
                           int d, void* dX, bool f32, const float* dw_partials, float* dA,
-                          float* dB, hipStream_t s);
+                          float* dB, hipStream_t s, bool fine = false);
 // dy_lo without x_lo: X is exact in bf16 and only dY has a low half.
-// fine: dWp and dA from G split into three bf16 parts instead of two.
+// fine (dX and dW): the d x d mix and dA on three bf16 parts instead of two.
 // dW reads the codes as the transposed code words r16t (launch_codes_to_r16t's layout).
 hipError_t launch_gemm_dw(const uint16_t* x, const uint16_t* x_lo, const uint16_t* dy,
                           const uint16_t* dy_lo, const uint32_t* r16t, const uint8_t* mask,

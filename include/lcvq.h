@@ -365,9 +365,8 @@ lcvq_status_t lcvq_mxfp4_gemv(const void* X, int64_t M, int64_t N, int64_t K, co
  * int8 [M, K] and Xs uint8 [M, K/32] in place of X; dt is the type of dY and dX. Every
  * other argument, the shapes and the errors are as for lcvq_linear_bwd (whose workspace this
  * call's can differ from). The gradients are those of the decoded X, which is exact in
- * bfloat16. dWp, dA and dB are formed from exact products, with the d x d mix on operands of
- * at least 24 bits (lcvq_linear_bwd: 16 bits); dX as by lcvq_linear_bwd, or for layers of few
- * tiles with the mix in float32, which rounds differently. With LCVQ_F32, dY is carried as a
+ * bfloat16. All four are formed from exact products and float32 sums, with the d x d mixes on
+ * operands of at least 24 bits (lcvq_linear_bwd: 16 bits). With LCVQ_F32, dY is carried as a
  * hi + lo pair (about 16 significant bits). Sums run in a fixed order: repeated calls give
  * identical bytes. A NaN block of X gives NaN gradients.
  */
