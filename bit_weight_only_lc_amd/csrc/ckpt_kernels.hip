@@ -11,7 +11,7 @@
 //     dB = G 1, are formed from G in LDS in float32.
 //   dX tile (m0, k0): C' = dY V over the outputs n, with V = 2 + z / 2, whose bf16 is a code
 //     moved to bits 5 and 6 of 2.0; C = 2 C' - 4 r and dX = C (I kron A^T) + r B, with r = dY 1
-//     summed from the same loads, in float32.
+//     summed from the same values, in float32.
 // A second launch adds the tiles' dA and dB sums in a fixed order. The contraction runs in
 // stages of 64, double-buffered in LDS; operands whose contraction runs along LDS rows are
 // read with the transposing 64-bit reads. float32 dY is carried as bf16 hi + lo.
@@ -125,10 +125,16 @@ template <> struct DyRaw<float> {
     put16<COLS>(hi, tid, pack16(h));
     put16<COLS>(lo, tid, pack16(l));
   }
+  // Of hi + lo, the values that the products take: in 2 C' - 4 r the 2 of each code's 2 + z / 2
+  // cancels only if both see the same dY (what the pair leaves of it, up to 2^-18, would weigh
+  // 4 + z). 1000 x 1024 x 4096, d = 4: 92 us, 89 with the plain sum.
   __device__ __forceinline__ float sum() const {
     float s = 0.f;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) s += (v[i][0] + v[i][1]) + (v[i][2] + v[i][3]);
+    for (int i = 0; i < 16; ++i) {
+      const float x = v[i >> 2][i & 3], h = (float)(__bf16)x;
+      s += h + (float)(__bf16)(x - h);
+    }
     return s;
   }
 };

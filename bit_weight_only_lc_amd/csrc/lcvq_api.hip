@@ -340,10 +340,10 @@ lcvq_status_t linear_bwd_impl(const void* dY, const void* X, const int8_t* Xc, c
   if (ckpt && bwd_prep_ckpt_blocks(f32, M, N, K) <= kMaxBlocks256) {
     e = launch_bwd_prep_ckpt(dY, Xc, Xs, f32, M, N, K, r, dy_hi, dy_lo, xd, packed, r16t, s);
   } else {
-    const bool merged = M + rblocks <= kMaxBlocks256;
+    const bool merged = !ckpt && M + rblocks <= kMaxBlocks256;
     e = merged ? launch_bwd_prep(dY, X, f32, M, N, K, r, dy_hi, dy_lo, x_hi, x_lo, packed, r16t,
                                  s)
-               : launch_bwd_prologue(dY, X, f32, M, N, K, r, dy_hi, dy_lo, x_hi, x_lo, s);
+               : launch_bwd_prologue(dY, X, f32, M, N, K, r, dy_hi, dy_lo, x_hi, x_lo, s, ckpt);
     if (e == hipSuccess && !merged) e = launch_codes_to_r16t(packed, N, K, r16t, s);
     if (e == hipSuccess && ckpt) e = launch_mx_dequantize(Xc, Xs, M * K, LCVQ_MXINT8, xd, false, s);
   }

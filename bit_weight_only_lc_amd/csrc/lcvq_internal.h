@@ -38,9 +38,10 @@ hipError_t launch_codes_to_r16t(const uint8_t* packed, int64_t N, int64_t K, uin
 hipError_t launch_fwd_prologue(const void* X, bool x_f32, int64_t M, int64_t K, const float* A,
                                const float* B, int d, uint16_t* xs, uint16_t* xs_lo,
                                float* beta, hipStream_t s);
+// pair: r of float32 dY sums the hi + lo pairs (as launch_bwd_prep_ckpt does).
 hipError_t launch_bwd_prologue(const void* dY, const void* X, bool f32, int64_t M, int64_t N,
                                int64_t K, float* r, uint16_t* dy_hi, uint16_t* dy_lo,
-                               uint16_t* x_hi, uint16_t* x_lo, hipStream_t s);
+                               uint16_t* x_hi, uint16_t* x_lo, hipStream_t s, bool pair = false);
 
 // One launch each for the forward's quantizer + prologue and the backward's prologue +
 // transposed codes (r16t may be NULL when dX is not wanted). Their grids are 256-thread

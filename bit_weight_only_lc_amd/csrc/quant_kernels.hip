@@ -402,7 +402,9 @@ __device__ __forceinline__ void split16(const float x[16], uint16_t* hi, uint16_
   dl[1] = make_uint4(l[4], l[5], l[6], l[7]);
 }
 
-template <typename T>
+// PAIR: r adds hi + lo, the values that the products take, instead of dY as it is: in dX's
+// 2 C' - 4 r the 2 of each code's 2 + z / 2 cancels only if both see the same dY.
+template <typename T, bool PAIR = false>
 __device__ __forceinline__ void bwd_prologue_body(int64_t m, const T* __restrict__ dY,
                                                   const T* __restrict__ X, int64_t N,
                                                   int64_t K, float* __restrict__ r,
@@ -417,7 +419,14 @@ __device__ __forceinline__ void bwd_prologue_body(int64_t m, const T* __restrict
     load16<T>(dY + m * N + c * 16, y);
     if (dy_hi) split16(y, dy_hi + m * N + c * 16, dy_lo + m * N + c * 16);
 #pragma unroll
-    for (int i = 0; i < 16; ++i) acc += y[i];
+    for (int i = 0; i < 16; ++i) {
+      if constexpr (PAIR) {
+        const float h = (float)(__bf16)y[i];
+        acc += h + (float)(__bf16)(y[i] - h);
+      } else {
+        acc += y[i];
+      }
+    }
   }
   if (x_hi) {
     for (int64_t c = threadIdx.x; c < (K >> 4); c += blockDim.x) {
@@ -538,7 +547,7 @@ __global__ __launch_bounds__(256) void k_bwd_prep_ckpt(const T* __restrict__ dY,
       const int64_t m = rb * 4 + (threadIdx.x >> 6);
       if (m < M) rowsum_bf16_wave(m, dY, N, r, threadIdx.x & 63);
     } else {
-      bwd_prologue_body<T>(rb, dY, nullptr, N, K, r, dy_hi, dy_lo, nullptr, nullptr);
+      bwd_prologue_body<T, true>(rb, dY, nullptr, N, K, r, dy_hi, dy_lo, nullptr, nullptr);
     }
   } else {
     const int64_t groups = M * K / 8;
@@ -561,7 +570,7 @@ __global__ __launch_bounds__(256) void k_bwd_prep_ckpt(const T* __restrict__ dY,
   }
 }
 
-template <typename T>
+template <typename T, bool PAIR>
 __global__ __launch_bounds__(256) void k_bwd_prologue(const T* __restrict__ dY,
                                                       const T* __restrict__ X, int64_t N,
                                                       int64_t K, float* __restrict__ r,
@@ -569,7 +578,7 @@ __global__ __launch_bounds__(256) void k_bwd_prologue(const T* __restrict__ dY,
                                                       uint16_t* __restrict__ dy_lo,
                                                       uint16_t* __restrict__ x_hi,
                                                       uint16_t* __restrict__ x_lo) {
-  bwd_prologue_body<T>(blockIdx.x, dY, X, N, K, r, dy_hi, dy_lo, x_hi, x_lo);
+  bwd_prologue_body<T, PAIR>(blockIdx.x, dY, X, N, K, r, dy_hi, dy_lo, x_hi, x_lo);
 }
 
 // ------------------------------------------------------------------ launchers
@@ -742,13 +751,17 @@ hipError_t launch_bwd_prep_ckpt(const void* dY, const int8_t* Xc, const uint8_t*
 
 hipError_t launch_bwd_prologue(const void* dY, const void* X, bool f32, int64_t M, int64_t N,
                                int64_t K, float* r, uint16_t* dy_hi, uint16_t* dy_lo,
-                               uint16_t* x_hi, uint16_t* x_lo, hipStream_t s) {
-  if (f32)
-    hipLaunchKernelGGL(k_bwd_prologue<float>, dim3((unsigned)M), dim3(256), 0, s,
-                       static_cast<const float*>(dY), static_cast<const float*>(X), N, K, r,
-                       dy_hi, dy_lo, x_hi, x_lo);
+                               uint16_t* x_hi, uint16_t* x_lo, hipStream_t s, bool pair) {
+  const float* y = static_cast<const float*>(dY);
+  const float* x = static_cast<const float*>(X);
+  if (f32 && pair)
+    hipLaunchKernelGGL((k_bwd_prologue<float, true>), dim3((unsigned)M), dim3(256), 0, s, y, x, N,
+                       K, r, dy_hi, dy_lo, x_hi, x_lo);
+  else if (f32)
+    hipLaunchKernelGGL((k_bwd_prologue<float, false>), dim3((unsigned)M), dim3(256), 0, s, y, x, N,
+                       K, r, dy_hi, dy_lo, x_hi, x_lo);
   else
-    hipLaunchKernelGGL(k_bwd_prologue<uint16_t>, dim3((unsigned)M), dim3(256), 0, s,
+    hipLaunchKernelGGL((k_bwd_prologue<uint16_t, false>), dim3((unsigned)M), dim3(256), 0, s,
                        static_cast<const uint16_t*>(dY), static_cast<const uint16_t*>(X), N,
                        K, r, (uint16_t*)nullptr, (uint16_t*)nullptr, (uint16_t*)nullptr,
                        (uint16_t*)nullptr);

@@ -76,3 +76,24 @@ def test_dx_mix_holds_24_bits(P, M, N, K, d):
     worst = float(((got.view_as(ref) - ref).abs() / mag).max())
     print(f"  {worst / U:.1f} U", flush=True)
     assert worst <= 36 * U
+
+
+@pytest.mark.parametrize("M,N,K", [(300, 320, 256), (4100, 1600, 2432)])
+def test_dx_of_float32_takes_one_dy(P, M, N, K):
+    """float32 dY goes into the products as a bfloat16 pair, about 16 bits. With A = I, B = 0
+    and one value per row, a multiple of 2^-20 below 2, every step of dX = z (hi + lo) is
+    exact (21 bits of the pair, 3 of a code); a row sum of the whole float32 dY would leave 4
+    times the rest of the pair in every element, codes 0 too."""
+    print("float32 dx", M, N, K, flush=True)
+    d = 8
+    packed, mask, _, _, z, _ = layer(P, N, K, d, 3)
+    A, B = torch.eye(d, device=DEV), torch.zeros(d, device=DEV)
+    g = torch.Generator(DEV).manual_seed(8)
+    at = torch.randint(0, N, (M, 1), generator=g, device=DEV)
+    v = torch.randint(-(1 << 21) + 1, 1 << 21, (M, 1), generator=g, device=DEV) / 2.0 ** 20
+    dY = torch.zeros(M, N, device=DEV).scatter_(1, at, v)
+    hi = v.to(BF).float()
+    pair = hi + (v - hi).to(BF).float()
+    assert (pair != v).any()
+    got = P.linear_bwd_ckpt8(dY, *checkpoint(P, M, K, 1), packed, mask, A, B, d)["dX"]
+    assert torch.equal(got, z[at.view(-1)].float() * pair)
