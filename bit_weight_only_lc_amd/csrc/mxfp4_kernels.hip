@@ -198,14 +198,17 @@ void k_mxfp4_tile(MxGemmArgs g) {
   const int64_t nb = g.nb, rowb = nb * 16;
 
   // The loads of this wave are buffer loads, whose range check gives zeros for rows past the
-  // matrix; a chunk past the row (the last stages) gets an offset outside every buffer.
-  const int64_t roww = n0 + wave * C::RW, rowx = m0 + wave * C::RX;
-  const int leftw = (int)max((int64_t)0, min(g.N - roww, (int64_t)C::RW));
-  const int leftx = (int)max((int64_t)0, min(g.M - rowx, (int64_t)C::RX));
-  const auto wsrc = __builtin_amdgcn_make_buffer_rsrc(
-      const_cast<uint8_t*>(g.Wc + (leftw ? roww * rowb : 0)), 0, (int)(leftw * rowb), 0x00020000);
-  const auto xsrc = __builtin_amdgcn_make_buffer_rsrc(
-      const_cast<uint8_t*>(g.Xc + (leftx ? rowx * rowb : 0)), 0, (int)(leftx * rowb), 0x00020000);
+  // matrix; a chunk past the row (the last stages) gets an offset outside every buffer. The
+  // check takes a stage's offset, added to all lanes, off the buffer's size, so a buffer is
+  // never shorter than a row: a wave past the matrix takes the last row, whose products are
+  // not stored.
+  const int64_t roww = min(n0 + wave * C::RW, g.N - 1), rowx = min(m0 + wave * C::RX, g.M - 1);
+  const int leftw = (int)min(g.N - roww, (int64_t)C::RW);
+  const int leftx = (int)min(g.M - rowx, (int64_t)C::RX);
+  const auto wsrc = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(g.Wc + roww * rowb), 0,
+                                                      (int)(leftw * rowb), 0x00020000);
+  const auto xsrc = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(g.Xc + rowx * rowb), 0,
+                                                      (int)(leftx * rowb), 0x00020000);
   const int rl = lane >> 2;
   const int chunk = (lane & 3) ^ ((rl >> 2) & 3);     // rows advance by 16 per load
   const uint32_t voff0 = (uint32_t)(rl * rowb + chunk * 16);
