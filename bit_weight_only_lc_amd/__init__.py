@@ -622,14 +622,18 @@ def mx_dequantize(codes, scales, fmt, dtype=torch.bfloat16):
 
 
 def mxfp4_linear(X, Wc, Ws, quantize_x=None):
-    """Y = X W^T (bf16) for a weight in MXFP4. quantize_x: X in MXFP4 too (lcvq_mxfp4_gemm)
-    or as it is (lcvq_mxfp4_gemv, up to 16 rows); by default as it is where that serves."""
+    """Y = X W^T (bf16) for a weight in MXFP4. X is 4 bits only where the caller says so:
+    quantize_x True   X in MXFP4 too (bf16 or float32, lcvq_mxfp4_gemm)
+    quantize_x False  X as it is, bf16, in one decode product (lcvq_mxfp4_gemv: 16 rows at most)
+    quantize_x None   X as it is, bf16, any number of rows: one decode product, which reads
+                      the weight once, for every 16."""
     M, N = X.shape[0], Wc.shape[0]
     Y = torch.empty((M, N), dtype=torch.bfloat16, device=X.device)
-    if quantize_x is None:
-        quantize_x = M > 16 or X.dtype != torch.bfloat16
     if quantize_x:
         lcvq_mxfp4_gemm(*mx_quantize(X, LCVQ_MXFP4), Wc, Ws, Y)
+    elif quantize_x is None and M > 16:
+        for m in range(0, M, 16):
+            lcvq_mxfp4_gemv(X[m:m + 16], Wc, Ws, Y[m:m + 16])
     else:
         lcvq_mxfp4_gemv(X, Wc, Ws, Y)
     return Y

@@ -56,7 +56,7 @@ class MLP:
             self.teacher[name] = P.mx_quantize(W, P.LCVQ_MXFP4)
 
     def teach(self, X, quantize_x=None):
-        """The 4-bit MLP; with quantize_x the activations are MXFP4 too."""
+        """The 4-bit MLP; the activations are MXFP4 too only with quantize_x (training)."""
         t = self.teacher
         G = P.mxfp4_linear(X, *t["gate"], quantize_x)
         U = P.mxfp4_linear(X, *t["up"], quantize_x)

@@ -70,3 +70,29 @@ def product(P, M, N, K, dt, seed=0):
 def test_waves_past_the_matrix(P, M, N, K, dt):
     """Tiles whose later waves have no row of W, of X, or of either."""
     product(P, M, N, K, dt)
+
+
+@pytest.mark.parametrize("M", [16, 17, 40])
+def test_linear_keeps_its_activations(P, M):
+    """mxfp4_linear's activations are those it was given, at any number of rows: against the
+    product of X itself (4-bit activations are off by 10% of it), and the same bytes as the
+    decode product of each 16 rows."""
+    N, K = 200, 416
+    X = values(M, K, 5).to(BF)
+    W = P.mx_quantize(values(N, K, 6), P.LCVQ_MXFP4)
+    Y = P.mxfp4_linear(X, *W)
+    Z, buf = guarded(M, N, BF)
+    for m in range(0, M, 16):
+        P.lcvq_mxfp4_gemv(X[m:m + 16], *W, Z[m:m + 16])
+    held(Z, buf, X.double(), decode(*W), f"linear {M}")
+    assert torch.equal(Y.view(torch.int16), Z.view(torch.int16))
+
+
+def test_linear_refuses_rather_than_quantise(P):
+    X = values(4, 64, 1)
+    W = P.mx_quantize(values(32, 64, 2), P.LCVQ_MXFP4)
+    with pytest.raises(TypeError):
+        P.mxfp4_linear(X, *W)                       # float32 activations
+    Y, Z = P.mxfp4_linear(X, *W, quantize_x=True), torch.empty(4, 32, dtype=BF, device=DEV)
+    P.lcvq_mxfp4_gemm(*P.mx_quantize(X, P.LCVQ_MXFP4), *W, Z)
+    assert torch.equal(Y, Z)
