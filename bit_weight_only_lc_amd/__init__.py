@@ -124,8 +124,13 @@ def _check(t, name, dtype=None, device=None):
         raise ValueError(f"{name} must be contiguous")
 
 
-# The handle alone of GPU i's current stream (building a torch.cuda.Stream object costs 2 us).
-_raw_stream = torch._C._cuda_getCurrentRawStream
+def _current_stream(i):
+    return torch.cuda.current_stream(i).cuda_stream
+
+
+# The handle alone of GPU i's current stream: building a torch.cuda.Stream object costs 2 us. A
+# torch without GPU support lacks the first name; the module is imported there all the same.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", _current_stream)
 
 
 def _stream(dev):

@@ -1,0 +1,39 @@
+"""The binding on a torch that lacks what only a GPU build of it has."""
+
+import os
+import subprocess
+import sys
+
+import pytest
+import torch
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+NAME = "_cuda_getCurrentRawStream"
+
+
+@pytest.fixture(scope="module")
+def built():
+    import bit_weight_only_lc_amd as P
+    if not os.path.exists(P.LIB_PATH):
+        from bit_weight_only_lc_amd import build
+        build.build()
+
+
+def test_import_without_the_raw_stream(built):
+    """The import, the sizes and the refusals of the C ABI need no GPU and no stream."""
+    code = (f"import torch\nif hasattr(torch._C, '{NAME}'): del torch._C.{NAME}\n"
+            "import bit_weight_only_lc_amd as P\n"
+            "assert P.lcvq_linear_bwd_ckpt8_workspace_size(16, 256, 256, 8) > 0\n"
+            "assert P.lib().lcvq_mxfp4_gemv(None, 1, 1, 32, None, None, None, None) == 1\n")
+    r = subprocess.run([sys.executable, "-c", code], cwd=ROOT, capture_output=True, text=True)
+    assert r.returncode == 0, r.stderr
+
+
+@pytest.mark.gpu
+def test_both_ways_name_the_same_stream():
+    import bit_weight_only_lc_amd as P
+    assert P._raw_stream is not P._current_stream
+    for s in (torch.cuda.current_stream(), torch.cuda.Stream()):
+        with torch.cuda.stream(s):
+            i = torch.cuda.current_device()
+            assert P._raw_stream(i) == P._current_stream(i) == s.cuda_stream
