@@ -413,14 +413,12 @@ def lcvq_mx_dequantize(codes, scales, fmt, out):
 
 
 def lcvq_mxfp4_gemm(Xc, Xs, Wc, Ws, Y, workspace=None):
-    """Y [M, N] (bf16 or float32) = X W^T, X [M, K] and W [N, K] in MXFP4."""
+    """Y [M, N] (bf16 or float32) = X W^T, X [M, K] and W [N, K] in MXFP4. (No workspace is
+    used; one that is given is checked.)"""
     i, M, N = _mat(Y, "Y")
     K = _mat(Wc, "W", (_U8,))[2] * 2
     _need_mx(Xc, Xs, "X", LCVQ_MXFP4, M, K, i)
     _need_mx(Wc, Ws, "W", LCVQ_MXFP4, N, K, i)
-    if workspace is None:
-        n = lcvq_mxfp4_gemm_workspace_size(M, N, K)
-        workspace = torch.empty(n, dtype=torch.uint8, device=Y.device) if n else None
     if workspace is not None:
         _need_workspace(workspace, i)
     _ok(lib().lcvq_mxfp4_gemm(Xc.data_ptr(), Xs.data_ptr(), M, N, K, Wc.data_ptr(),

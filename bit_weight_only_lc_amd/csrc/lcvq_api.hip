@@ -517,25 +517,20 @@ lcvq_status_t lcvq_mx_dequantize(const void* codes, const uint8_t* scales, int64
                                        as_stream(stream)));
 }
 
-size_t lcvq_mxfp4_gemm_workspace_size(int64_t M, int64_t N, int64_t K) {
-  if (!mxfp4_gemm_shape_ok(M, N, K)) return 0;
-  return mxfp4_gemm_ws_bytes(M, N, K);
-}
+size_t lcvq_mxfp4_gemm_workspace_size(int64_t, int64_t, int64_t) { return 0; }
 
 lcvq_status_t lcvq_mxfp4_gemm(const void* Xc, const uint8_t* Xs, int64_t M, int64_t N, int64_t K,
                               const void* Wc, const uint8_t* Ws, void* Y, lcvq_dtype_t ydt,
-                              void* workspace, size_t workspace_bytes, void* stream) {
+                              void* workspace, size_t, void* stream) {
   if (!Xc || !Xs || !Wc || !Ws || !Y) return LCVQ_ERR_NULL;
   if (!dt_ok(ydt)) return LCVQ_ERR_DTYPE;
   if (!mxfp4_gemm_shape_ok(M, N, K)) return LCVQ_ERR_SHAPE;
   if (!aligned16(Xc) || !aligned16(Xs) || !aligned16(Wc) || !aligned16(Ws) || !aligned16(Y) ||
       !aligned16(workspace))
     return LCVQ_ERR_ALIGN;
-  const size_t need = mxfp4_gemm_ws_bytes(M, N, K);
-  if (need && (!workspace || workspace_bytes < need)) return LCVQ_ERR_WORKSPACE;
   return from_hip(launch_mxfp4_gemm(static_cast<const uint8_t*>(Xc), Xs, M, N, K,
                                     static_cast<const uint8_t*>(Wc), Ws, Y, ydt == LCVQ_F32,
-                                    workspace, as_stream(stream)));
+                                    as_stream(stream)));
 }
 
 lcvq_status_t lcvq_mxfp4_gemv(const void* X, int64_t M, int64_t N, int64_t K, const void* Wc,

@@ -133,11 +133,10 @@ hipError_t launch_silu_gate_fwd(const void* G, const void* U, bool f32, int64_t 
 hipError_t launch_silu_gate_bwd(const void* dH, bool f32, int64_t n, const int8_t* Gc,
                                 const uint8_t* Gs, const int8_t* Uc, const uint8_t* Us, void* dG,
                                 void* dU, hipStream_t s);
-// MXFP4 products; the gemm's workspace holds split-contraction partials (0 bytes: none).
-size_t mxfp4_gemm_ws_bytes(int64_t M, int64_t N, int64_t K);
+// MXFP4 products.
 hipError_t launch_mxfp4_gemm(const uint8_t* Xc, const uint8_t* Xs, int64_t M, int64_t N,
                              int64_t K, const uint8_t* Wc, const uint8_t* Ws, void* Y, bool y_f32,
-                             void* split_ws, hipStream_t s);
+                             hipStream_t s);
 hipError_t launch_mxfp4_gemv(const uint16_t* X, int M, int64_t N, int64_t K, const uint8_t* Wc,
                              const uint8_t* Ws, uint16_t* Y, hipStream_t s);
 

@@ -771,8 +771,6 @@ __global__ __launch_bounds__(mx_skinny_waves(XR, RG) * 64) void k_mxfp4_skinny(M
   }
 }
 
-size_t mxfp4_gemm_ws_bytes(int64_t, int64_t, int64_t) { return 0; }
-
 template <typename T, int WI, int WJ, int NWN, int NWM, int RING>
 static hipError_t launch_tile(MxGemmArgs g, hipStream_t s) {
   using C = MxTile<WI, WJ, NWN, NWM, RING>;
@@ -816,8 +814,7 @@ static hipError_t tile_typed(const MxGemmArgs& g, bool y_f32, hipStream_t s) {
 
 hipError_t launch_mxfp4_gemm(const uint8_t* Xc, const uint8_t* Xs, int64_t M, int64_t N,
                              int64_t K, const uint8_t* Wc, const uint8_t* Ws, void* Y, bool y_f32,
-                             void* split_ws, hipStream_t s) {
-  (void)split_ws;
+                             hipStream_t s) {
   const MxSkinnyArgs k{Xc, Xs, Wc, Ws, (int)std::min<int64_t>(M, 64), N, K / MXB, Y};
   if (M <= 16) return y_f32 ? skinny_rows<0, float, 1>(k, s) : skinny_rows<0, uint16_t, 1>(k, s);
   if (M <= 32) return y_f32 ? skinny_rows<0, float, 2>(k, s) : skinny_rows<0, uint16_t, 2>(k, s);

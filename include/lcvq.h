@@ -333,14 +333,13 @@ lcvq_status_t lcvq_mx_dequantize(const void* codes, const uint8_t* scales, int64
  *   Y  [M, N] in ydt                                                          out
  *   1 <= M, N <= 2^24, any values; K a multiple of 32 up to 2^21; M * K, N * K and
  *   M * N < 2^40; at most 2^23 - 8 tiles of 256 x 256 in Y
- *   workspace >= lcvq_mxfp4_gemm_workspace_size(M, N, K) bytes (0: may be NULL)
+ *   workspace, workspace_bytes: not used; lcvq_mxfp4_gemm_workspace_size is 0 for every shape.
+ *   NULL, or 16-byte aligned.
  *   Xs and Ws are read in aligned 4-byte words, the last of which may reach up to 3 bytes past
  *   the array (never into another page, and the bytes do not matter)
- * Numerics: 4-bit matrix cores with float32 accumulation; sums over a split contraction
- * are added in a fixed order, so repeated calls give identical bytes. A row of X (of W) with
- * a NaN block gives NaN in its row (column) of Y.
- * Errors: LCVQ_ERR_NULL, LCVQ_ERR_DTYPE, LCVQ_ERR_SHAPE, LCVQ_ERR_ALIGN,
- * LCVQ_ERR_WORKSPACE, LCVQ_ERR_HIP.
+ * Numerics: 4-bit matrix cores with float32 accumulation in a fixed order, so repeated calls
+ * give identical bytes. A row of X (of W) with a NaN block gives NaN in its row (column) of Y.
+ * Errors: LCVQ_ERR_NULL, LCVQ_ERR_DTYPE, LCVQ_ERR_SHAPE, LCVQ_ERR_ALIGN, LCVQ_ERR_HIP.
  */
 size_t lcvq_mxfp4_gemm_workspace_size(int64_t M, int64_t N, int64_t K);
 lcvq_status_t lcvq_mxfp4_gemm(const void* Xc, const uint8_t* Xs, int64_t M, int64_t N, int64_t K,

@@ -1,4 +1,4 @@
-"""The binding on a torch that lacks what only a GPU build of it has."""
+"""The block-scaled binding: what it needs of torch, and of a workspace."""
 
 import os
 import subprocess
@@ -27,6 +27,26 @@ def test_import_without_the_raw_stream(built):
             "assert P.lib().lcvq_mxfp4_gemv(None, 1, 1, 32, None, None, None, None) == 1\n")
     r = subprocess.run([sys.executable, "-c", code], cwd=ROOT, capture_output=True, text=True)
     assert r.returncode == 0, r.stderr
+
+
+@pytest.mark.parametrize("M,N,K", [(1, 64, 14336), (16, 1, 32), (64, 4096, 14336),
+                                   (4096, 4096, 4096), (1 << 20, 1 << 16, 4096), (0, 5, 64)])
+def test_product_needs_no_workspace(built, M, N, K):
+    import bit_weight_only_lc_amd as P
+    assert P.lcvq_mxfp4_gemm_workspace_size(M, N, K) == 0
+
+
+@pytest.mark.gpu
+def test_product_ignores_its_workspace():
+    """NULL, one byte and a large workspace give the same bytes, and leave it as it is."""
+    import bit_weight_only_lc_amd as P
+    X, W = (P.mx_quantize(torch.randn(r, 512, device="cuda"), P.LCVQ_MXFP4) for r in (70, 90))
+    Y = torch.empty(70, 90, dtype=torch.bfloat16, device="cuda")
+    P.lcvq_mxfp4_gemm(*X, *W, Y)
+    for n in (1, 1 << 20):
+        ws, Z = torch.full((n,), 7, dtype=torch.uint8, device="cuda"), torch.zeros_like(Y)
+        P.lcvq_mxfp4_gemm(*X, *W, Z, ws)
+        assert torch.equal(Y, Z) and bool((ws == 7).all())
 
 
 @pytest.mark.gpu
