@@ -8,7 +8,10 @@ namespace lcvq {
 // Kernel ids of the profiling hook (lcvq_profile_next).
 enum { PROF_QUANTIZE = 1, PROF_FWD = 2, PROF_DX = 3, PROF_DW = 4, PROF_GEMV = 5, PROF_BWD_PREP = 6,
        PROF_GRAM = 7, PROF_PTQ_SWEEP = 8, PROF_READ_PROBE = 9,
-       PROF_MFMA_PROBE = 10, PROF_PACK = 11, PROF_UNPACK = 12, PROF_LAST = 12 };
+       PROF_MFMA_PROBE = 10, PROF_PACK = 11, PROF_UNPACK = 12, PROF_LAST = 12,
+       // the MXFP4 products
+       PROF_MX_FEW = 20, PROF_MX_64 = 21, PROF_MX_64_128 = 22, PROF_MX_128 = 23, PROF_MX_256 = 24,
+       PROF_MX_GEMV = 25 };
 // True (once) if the calling thread armed timing for kernel `id`; returns the events.
 bool take_profile(int id, hipEvent_t* start, hipEvent_t* stop);
 

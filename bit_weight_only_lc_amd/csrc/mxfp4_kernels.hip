@@ -778,20 +778,24 @@ static hipError_t launch_tile(MxGemmArgs g, hipStream_t s) {
   g.tilesM = (int)((g.M + C::BM - 1) / C::BM);
   g.ntiles = g.tilesN * g.tilesM;
   const dim3 grid((unsigned)((g.ntiles + 7) / 8 * 8)), block(C::NW * 64);
+  constexpr int id = C::BN == 256   ? PROF_MX_256
+                     : C::BN == 128 ? PROF_MX_128
+                     : C::BM == 128 ? PROF_MX_64_128 : PROF_MX_64;
   if (g.nb % 4 == 0)
-    hipLaunchKernelGGL((k_mxfp4_tile<T, WI, WJ, NWN, NWM, RING, true>), grid, block, 0, s, g);
+    LCVQ_LAUNCH(id, (k_mxfp4_tile<T, WI, WJ, NWN, NWM, RING, true>), grid, block, 0, s, g);
   else
-    hipLaunchKernelGGL((k_mxfp4_tile<T, WI, WJ, NWN, NWM, RING, false>), grid, block, 0, s, g);
+    LCVQ_LAUNCH(id, (k_mxfp4_tile<T, WI, WJ, NWN, NWM, RING, false>), grid, block, 0, s, g);
   return hipGetLastError();
 }
 
 template <int XR, typename T, int MB, int RG>
 static hipError_t launch_skinny(const MxSkinnyArgs& g, hipStream_t s) {
   const dim3 grid((unsigned)((g.N + 16 * RG - 1) / (16 * RG))), block(mx_skinny_waves(XR, RG) * 64);
+  constexpr int id = XR ? PROF_MX_GEMV : PROF_MX_FEW;
   if (g.nb % 4 == 0)
-    hipLaunchKernelGGL((k_mxfp4_skinny<XR, T, MB, RG, true>), grid, block, 0, s, g);
+    LCVQ_LAUNCH(id, (k_mxfp4_skinny<XR, T, MB, RG, true>), grid, block, 0, s, g);
   else
-    hipLaunchKernelGGL((k_mxfp4_skinny<XR, T, MB, RG, false>), grid, block, 0, s, g);
+    LCVQ_LAUNCH(id, (k_mxfp4_skinny<XR, T, MB, RG, false>), grid, block, 0, s, g);
   return hipGetLastError();
 }
 

@@ -432,7 +432,8 @@ lcvq_status_t lcvq_mfma_probe(int64_t iters, uint32_t* sink, void* stream);
  * 6 backward prologue (r = dY 1 and the transposed codes, lcvq_linear_bwd), 7 Gram
  * product (lcvq_hessian), 8 PTQ integer step (lcvq_ptq_init; each call times the first),
  * 9 read probe (lcvq_read_probe), 10 MFMA probe (lcvq_mfma_probe), 11 packer
- * (lcvq_pack2b), 12 unpacker (lcvq_unpack2b).
+ * (lcvq_pack2b), 12 unpacker (lcvq_unpack2b); lcvq_mxfp4_gemm's kernels: 20 few rows, 21 tiles
+ * of 64 x 64, 22 of 64 rows of W by 128 of X, 23 of 128 x 128, 24 of 256 x 256; 25 lcvq_mxfp4_gemv.
  * Passing NULL events disarms. Returns LCVQ_ERR_SHAPE for an unknown kernel_id.
  */
 lcvq_status_t lcvq_profile_next(int kernel_id, void* start_event, void* stop_event);

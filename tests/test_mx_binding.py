@@ -36,6 +36,13 @@ def test_product_needs_no_workspace(built, M, N, K):
     assert P.lcvq_mxfp4_gemm_workspace_size(M, N, K) == 0
 
 
+def test_profile_hook_ids_of_the_products(built):
+    """Ids 20 to 25 name their kernels; none lies on either side (no GPU call)."""
+    import bit_weight_only_lc_amd as P
+    for kid in range(13, 33):
+        assert P.lib().lcvq_profile_next(kid, None, None) == (0 if 20 <= kid <= 25 else 2)
+
+
 @pytest.mark.gpu
 def test_product_ignores_its_workspace():
     """NULL, one byte and a large workspace give the same bytes, and leave it as it is."""
