@@ -226,9 +226,12 @@ __global__ __launch_bounds__(256) void k_bwd8_small(Bwd8Args a) {
   float* g = reinterpret_cast<float*>(smem);                 // epilogue tiles
   float* z = g + ST * GS;
   const T* dY = static_cast<const T*>(a.dY);
-  f32x16 acc[NB];
+  // float32: dY's low halves in sums of their own. Added to the large ones each product would be
+  // rounded against them, toward one side (dB of 1000 tokens, 2048 x 2496: 8e-6, so 3e-7).
+  constexpr int NA = F32 ? 2 * NB : NB;
+  f32x16 acc[NA];
 #pragma unroll
-  for (int b = 0; b < NB; ++b)
+  for (int b = 0; b < NA; ++b)
 #pragma unroll
     for (int r = 0; r < 16; ++r) acc[b][r] = 0.f;
 
@@ -272,7 +275,7 @@ __global__ __launch_bounds__(256) void k_bwd8_small(Bwd8Args a) {
           const uint8_t* y = t + TB + b * YB;
           acc[b] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(x, frag_cols(y, q0, s, lane), acc[b], 0, 0, 0);
           if constexpr (F32)
-            acc[b] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(x, frag_cols(y + TB, q0, s, lane), acc[b], 0, 0, 0);
+            acc[NB + b] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(x, frag_cols(y + TB, q0, s, lane), acc[NB + b], 0, 0, 0);
         }
       }
     }, smem, SB);
@@ -281,6 +284,7 @@ __global__ __launch_bounds__(256) void k_bwd8_small(Bwd8Args a) {
       if (n0 + b * ST >= a.N) break;
       __syncthreads();
       // G as [n][k] and the codes as float32
+      if constexpr (F32) acc[b] += acc[NB + b];
       put_block<true>(g, acc[b], p0, q0, lane);
       const int64_t n = n0 + b * ST + row;
       const uint32_t code = *reinterpret_cast<const uint32_t*>(a.packed + n * (a.K / 4) + (k0 + c16) / 4);
@@ -358,7 +362,7 @@ __global__ __launch_bounds__(256) void k_bwd8_small(Bwd8Args a) {
           const uint8_t* y = t + TB + b * YB;
           acc[b] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(frag_rows(y, p0, s, lane), zf, acc[b], 0, 0, 0);
           if constexpr (F32)
-            acc[b] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(frag_rows(y + TB, p0, s, lane), zf, acc[b], 0, 0, 0);
+            acc[NB + b] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(frag_rows(y + TB, p0, s, lane), zf, acc[NB + b], 0, 0, 0);
         }
       }
     }, smem, SB);
@@ -369,6 +373,7 @@ __global__ __launch_bounds__(256) void k_bwd8_small(Bwd8Args a) {
       float r = rsum[b];
       r += __shfl_xor(r, 1);
       r += __shfl_xor(r, 2);
+      if constexpr (F32) acc[b] += acc[NB + b];
       put_block<false>(g, acc[b], p0, q0, lane);                  // C as [m][k]
       __syncthreads();
       float v[16], o[16];

@@ -1959,7 +1959,8 @@ hipError_t launch_gemm_dx(const uint32_t* r16t, const uint16_t* dy, const uint16
   a.splits = 1;
   a.P = K; a.Q = M; a.R = N;
   a.codes = r16t;
-  a.Rmat[0] = dy; a.Rmat[1] = dy_lo;
+  a.Rmat[0] = fine && dy_lo ? dy_lo : dy;    // (lo first: see launch_gemm_dw)
+  a.Rmat[1] = fine ? dy : dy_lo;
   a.npass = dy_lo ? 2 : 1;
   a.rowvec = r; a.A = A; a.B = B;
   a.M = M; a.N = N; a.K = K;
@@ -1986,8 +1987,12 @@ hipError_t launch_gemm_dw(const uint16_t* x, const uint16_t* x_lo, const uint16_
     a.Lmat[1] = x_lo; a.Rmat[1] = dy;
     a.Lmat[2] = x; a.Rmat[2] = dy_lo;
     a.npass = 3;
-  } else if (dy_lo) {         // X exact in bf16: hi*hi + hi*lo
-    a.Lmat[1] = x; a.Rmat[1] = dy_lo;
+  } else if (dy_lo) {
+    // X exact in bf16: lo, then hi. The other way round each of the low products would be
+    // rounded against the large sums, toward one side: dA and dB, which add up millions of
+    // the sums, came to 1e-5 of their size (4100 tokens, 1600 x 2432; now 1.5e-6).
+    a.Rmat[0] = dy_lo;
+    a.Lmat[1] = x; a.Rmat[1] = dy;
     a.npass = 2;
   }
   a.A = A;

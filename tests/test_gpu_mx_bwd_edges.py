@@ -4,6 +4,8 @@ The operators' formulas are evaluated in float64 with torch. Tolerances are coun
 arithmetic before the bound; U = 2^-24 is half a unit of float32.
 """
 
+import time
+
 import pytest
 import torch
 
@@ -97,3 +99,110 @@ def test_dx_of_float32_takes_one_dy(P, M, N, K):
     assert (pair != v).any()
     got = P.linear_bwd_ckpt8(dY, *checkpoint(P, M, K, 1), packed, mask, A, B, d)["dX"]
     assert torch.equal(got, z[at.view(-1)].float() * pair)
+
+
+def launches_prologue(P, call):
+    """Whether call() took the 256 x 256 tiles, whose prologue the library's profiling hook
+    knows (id 6): its two events lie 20 ms apart before."""
+    a, b = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+    a.record()
+    time.sleep(0.02)
+    b.record()
+    torch.cuda.synchronize()
+    assert P.lib().lcvq_profile_next(6, a.cuda_event, b.cuda_event) == 0
+    call()
+    assert P.lib().lcvq_profile_next(6, None, None) == 0
+    torch.cuda.synchronize()
+    return a.elapsed_time(b) < 15
+
+
+def held(got, ref, tol, label):
+    """floatcheck's three figures (tensor, 32 x 32 blocks, elements), on the GPU."""
+    got = got.double().view(-1, got.shape[-1])
+    ref = ref.view_as(got)
+    assert bool(torch.isfinite(got).all()), label
+    e = got - ref
+    rms = float(ref.square().mean().sqrt())
+
+    def blocks(x):
+        x = torch.nn.functional.pad(x.square(), (0, -x.shape[1] % 32, 0, -x.shape[0] % 32))
+        return x.view(x.shape[0] // 32, 32, -1, 32).sum((1, 3)).sqrt()
+
+    den = blocks(ref).maximum(1e-3 * rms * blocks(torch.ones_like(ref)))
+    figures = (float(e.norm() / ref.norm()), float((blocks(e) / den).max()),
+               float((e.abs() / (ref.abs() + 4 * rms)).max()))
+    print(f"  {label} {figures[0]:.1e} {figures[1]:.1e} {figures[2]:.1e}", flush=True)
+    assert max(figures) <= tol, (label, figures)
+
+
+def carried(dY):
+    """The values the products take for dY: float32 as a bfloat16 pair."""
+    hi = dY.to(BF).float()
+    return (hi + (dY.float() - hi).to(BF).float()).double()
+
+
+def formulas(dY, X, z, m, A, B, d):
+    y, zd, Ad = carried(dY), z.double(), A.double()
+    N, K = z.shape
+    What = (zd.view(-1, d) @ Ad.t() + B.double()).view(N, K)
+    G = y.t() @ X
+    g = G.view(-1, d)
+    return {"dX": y @ What, "dWp": (g @ Ad).view(N, K) * m, "dA": g.t() @ zd.view(-1, d),
+            "dB": g.sum(0)}
+
+
+# The kernels that a layer takes, by the launch rules:
+#   dW in 256 x 256 tiles: more than 128 of them, one workgroup per tile; up to 128, split over
+#     the tokens, with a second launch; more than 256, a multiple of 8, that leave a last round
+#     at most half full, from 961 tokens on, the last ones split
+#   dX in the same tiles; 64 x 64 tiles for both up to 60000 blocks of 64^3, float32 45000
+UNSPLIT, SPLIT, TAIL = (1030, 3904, 4032), (4100, 1600, 2432), (1030, 4544, 4096)
+LARGE = [(s, d, dt) for s in (UNSPLIT, SPLIT, TAIL) for d in (4, 8, 16) for dt in (BF, F32)]
+SMALL = [((70, 192, 320), d, dt) for d in (4, 8, 16) for dt in (BF, F32)] + \
+        [((2050, 2112, 1984), d, BF) for d in (4, 8, 16)] + \
+        [((4100, 1344, 2048), d, F32) for d in (4, 8, 16)]       # (bfloat16: two tiles of dY per workgroup)
+
+
+def run(P, shape, d, dt, want_dx=True):
+    M, N, K = shape
+    print("bwd", shape, d, dt, "" if want_dx else "without dX", flush=True)
+    packed, mask, A, B, z, m = layer(P, N, K, d, M + d)
+    g = torch.Generator(DEV).manual_seed(M)
+    dY = torch.randn(M, N, generator=g, device=DEV).to(dt)
+    xc, xs = checkpoint(P, M, K, 2)
+    out = {}
+
+    def call():
+        out.update(P.linear_bwd_ckpt8(dY, xc, xs, packed, mask, A, B, d, want_dx))
+    large = launches_prologue(P, call)
+    first = {n: t.clone() for n, t in out.items() if t is not None}
+    call()
+    assert all(torch.equal(out[n], t) for n, t in first.items())
+    X = P.mx_dequantize(xc, xs, P.LCVQ_MXINT8, F32).double()
+    ref = formulas(dY, X, z, m, A, B, d)
+    # exact products and operands of 24 bits: float32 sums of up to 4608 terms, 1e-5 is 100
+    # units of their result's size; bfloat16 dX is rounded once more, by half a unit
+    for n, t in first.items():
+        held(t, ref[n], 2.0 ** -8 * 1.01 if n == "dX" and dt == BF else 1e-5, n)
+    return large
+
+
+@pytest.mark.parametrize("shape,d,dt", LARGE)
+def test_large_layers(P, shape, d, dt):
+    assert run(P, shape, d, dt)
+
+
+@pytest.mark.parametrize("shape,d,dt", SMALL)
+def test_layers_of_few_tiles(P, shape, d, dt):
+    assert not run(P, shape, d, dt)
+
+
+# without dX the rule counts dW's tiles of 64 x 64 too: 1536 of them; float32 20000 blocks
+@pytest.mark.parametrize("shape,d,dt,large", [((70, 2496, 2496), 8, BF, False),
+                                              ((70, 2560, 2560), 16, BF, True),
+                                              ((1, 2560, 2560), 8, BF, True),
+                                              ((1000, 2048, 2496), 4, F32, False),
+                                              ((1030, 2048, 2496), 8, F32, True),
+                                              ((1030, 4544, 4096), 8, BF, True)])
+def test_without_dx(P, shape, d, dt, large):
+    assert run(P, shape, d, dt, want_dx=False) == large
