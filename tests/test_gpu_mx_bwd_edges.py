@@ -206,3 +206,26 @@ def test_layers_of_few_tiles(P, shape, d, dt):
                                               ((1030, 4544, 4096), 8, BF, True)])
 def test_without_dx(P, shape, d, dt, large):
     assert run(P, shape, d, dt, want_dx=False) == large
+
+
+@pytest.mark.parametrize("shape", [(70, 192, 320), (2050, 2112, 1984), UNSPLIT, SPLIT, TAIL])
+@pytest.mark.parametrize("d", [8, 16])
+def test_nan_block_of_a_checkpoint(P, shape, d):
+    """It reaches dWp of its 32 columns, all of dA and dB, and nothing else: dX and the other
+    columns are those of the same call without it."""
+    M, N, K = shape
+    print("nan block", shape, d, flush=True)
+    packed, mask, A, B, _, m = layer(P, N, K, d, 7)
+    g = torch.Generator(DEV).manual_seed(M)
+    dY = torch.randn(M, N, generator=g, device=DEV).to(BF)
+    xc, xs = checkpoint(P, M, K, 4)
+    xc[M - 1, 96:128] = 0
+    want = P.linear_bwd_ckpt8(dY, xc, xs, packed, mask, A, B, d)
+    xs[M - 1, 3] = 255
+    got = P.linear_bwd_ckpt8(dY, xc, xs, packed, mask, A, B, d)
+    assert torch.equal(got["dX"], want["dX"])
+    block = torch.zeros(K, dtype=torch.bool, device=DEV)
+    block[96:128] = True
+    assert torch.equal(got["dWp"][:, ~block], want["dWp"][:, ~block])
+    assert bool(torch.isnan(got["dWp"][:, block][m[:, block]]).all())
+    assert bool(torch.isnan(got["dA"]).all()) and bool(torch.isnan(got["dB"]).all())
