@@ -1,7 +1,7 @@
 // Block-scaled storage of activations and weights, and the SiLU gate that keeps its
 // operands in it. All of these read and write each value once and are bound by HBM: bf16 at
-// 8192 x 11008, gate forward with three checkpoints 144 us (0.82 GB, 5.7 TB/s), backward
-// 125 us (0.73 GB, 5.8 TB/s), MXINT8 quantisation of 8192 x 14336 70 us (0.36 GB, 5.1 TB/s);
+// 8192 x 11008, gate forward with three checkpoints 139 us (0.82 GB, 5.9 TB/s), backward
+// 132 us (0.73 GB, 5.5 TB/s), MXINT8 quantisation of 8192 x 14336 69 us (0.36 GB, 5.1 TB/s);
 // a copy of 1 GiB reaches 5.2 TB/s, of 256 MiB 5.5.
 // Rows are made of whole blocks of 32, so a matrix is a flat run of blocks; a lane takes 8
 // consecutive values and four lanes share a block.

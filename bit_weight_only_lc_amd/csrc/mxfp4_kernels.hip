@@ -90,10 +90,10 @@ template <bool AL> struct MxScaleTail {
 // cover the 64 banks once. Scale bytes come 16 per row and 512 values through registers
 // into a double-buffered LDS area; a wave reads the 4 bytes of a stage as one word and
 // moves the byte of its half (blocks 2s + h, h = lane / 32) to bytes 0 and 2.
-// Large products are bound by the matrix units' power: 8192 x 14336 x 4096 267 us, 3.6 PFLOP/s
-// (8192^3: 273 us on random values at 1.84 GHz, 204 us on zeros). At one tile of 128 x 128 per
-// CU or fewer a stage takes 0.3 us, 256 cycles of products and 384 of LDS that nothing
-// overlaps, and filling and emptying the pipeline 4 us (512 x 4096 x 4096: 12.7 us).
+// Large products are bound by the matrix units' power: 8192 x 14336 x 4096 259 us, 3.7 PFLOP/s
+// (8192^3: 268 us on random values, 203 us on zeros). At one tile of 128 x 128 per CU or
+// fewer a stage takes 0.3 us, 256 cycles of products and 384 of LDS that nothing overlaps,
+// and filling and emptying the pipeline 4 us (1024 x 4096 x 4096: 13.1 us).
 constexpr int MXK = 128;                       // values per stage
 constexpr int MXROWB = MXK / 2;                // bytes per row and stage
 
@@ -828,11 +828,11 @@ hipError_t launch_mxfp4_gemm(const uint8_t* Xc, const uint8_t* Xs, int64_t M, in
   g.Y = Y;
   // Tiles: 256 x 256 where more than half of the 256 CUs get one; else the largest of which
   // a smaller one would give a CU more than one: 64 x 64, 64 rows of W by 128 of X, 128 x 128.
-  // (K = 4096: 2048 x 4096 29.8 us with 256, 30.9 with 128; 1024 x 4096 27.6, 16.4, 21.3 with
-  // 64 x 128; 512 x 4096 13.1 with 128, 11.9 with 64 x 128; 128 x 14336 13.4, 12.2, 14.0 with
-  // 64; 256 x 4096 12.5, 11.2, 8.7.) One small tile per CU needs eight slots for its loads to
-  // be on time (64 x 4096 x 14336: 26.2 us with four, 20.5); for the larger the longer fill
-  // costs as much as it gives (512 x 4096 x 4096, 128: 13.2 us with four, 13.6).
+  // (K = 4096, with 256 / 128 / 64 x 128 / 64: 2048 x 4096 28.4 us, 26.8; 1024 x 4096 24.4,
+  // 13.1, 18.7; 512 x 4096 23.9, 10.7, 10.4, 12.9; 128 x 14336 with 128 on: 11.4, 10.7, 12.4;
+  // 256 x 4096 9.8, 9.3, 7.9.) One small tile per CU needs eight slots for its loads to be on
+  // time (64 x 4096 x 14336: 24.7 us with four, 17.6); for the larger the longer fill costs
+  // as much as it gives (515 x 4001 x 4128, 128: 16.0 us with four, 16.9).
   auto tiles = [&](int64_t n, int64_t m) { return ((M + m - 1) / m) * ((N + n - 1) / n); };
   if (tiles(256, 256) > 128) return tile_typed<4, 4, 4>(g, y_f32, s);
   if (tiles(64, 64) <= 256) return tile_typed<1, 1, 8>(g, y_f32, s);

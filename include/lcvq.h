@@ -366,8 +366,10 @@ lcvq_status_t lcvq_mxfp4_gemv(const void* X, int64_t M, int64_t N, int64_t K, co
  * call's can differ from). The gradients are those of the decoded X, which is exact in
  * bfloat16. All four are formed from exact products and float32 sums, with the d x d mixes on
  * operands of at least 24 bits (lcvq_linear_bwd: 16 bits). With LCVQ_F32, dY is carried as a
- * hi + lo pair (about 16 significant bits), the same in every sum. Sums run in a fixed order: repeated calls give
- * identical bytes. A NaN block of X gives NaN gradients.
+ * hi + lo pair (about 16 significant bits, as by lcvq_linear_bwd: a third part would cost half
+ * as much again), the same in every sum. Sums run in a fixed order: repeated calls give
+ * identical bytes. A NaN block of X gives NaN in dA, dB and, where the mask lets them through,
+ * its 32 columns of dWp, and changes nothing else.
  */
 size_t lcvq_linear_bwd_ckpt8_workspace_size(int64_t M, int64_t N, int64_t K, int d);
 lcvq_status_t lcvq_linear_bwd_ckpt8(const void* dY, const int8_t* Xc, const uint8_t* Xs,
